@@ -186,6 +186,22 @@ def _addr(t, name, dtype, device, shape):
     return t.data_ptr()
 
 
+def _ws(ws, device):
+    """Address and size of a workspace that the caller gives."""
+    if not isinstance(ws, torch.Tensor):
+        raise TypeError("ws must be a tensor")
+    if not (ws.is_cuda and ws.device == device and ws.is_contiguous()):
+        raise ValueError(f"ws must be a contiguous tensor on {device}")
+    return ws.data_ptr(), ws.numel()
+
+
+def _index_list(idx, name, num_q, device):
+    """(address, k) of an index list of at least num_q rows."""
+    if not isinstance(idx, torch.Tensor) or idx.dim() != 2 or idx.shape[0] < num_q:
+        raise ValueError(f"{name} must be a tensor [{num_q}, k]")
+    return _addr(idx, name, torch.int32, device, idx.shape), idx.shape[1]
+
+
 class Batch:
     """Batch layout (dsa_batch_t): query rows of sequence b are
     [q_start[b], q_start[b+1]); query t sits at position q_pos[t]; position s
@@ -362,19 +378,17 @@ def dsa_sparse_mla_attn(q_lat, q_rope, kv, idx, batch: Batch, *, scale: float, o
     pr = _addr(q_rope, "q_rope", torch.bfloat16, dev, (nq, H, ROPE))
     dt = _kv_dtype(kv)
     pkv = _addr(kv, "kv", kv.dtype, dev, kv.shape)
-    if not isinstance(idx, torch.Tensor) or idx.dim() != 2 or idx.shape[0] < nq:
-        raise ValueError(f"idx must be a tensor [{nq}, k]")
-    k = idx.shape[1]
-    pi = _addr(idx, "idx", torch.int32, dev, idx.shape)
+    pi, k = _index_list(idx, "idx", nq, dev)
     if out is None:
         out = _made(stream, torch.empty, (nq, H, LATENT), dtype=torch.bfloat16, device=dev)
     po = _addr(out, "out", torch.bfloat16, dev, (nq, H, LATENT))
     if lse is None and with_lse:
         lse = _made(stream, torch.empty, (nq, H), dtype=torch.float32, device=dev)
+    pl = None if lse is None else _addr(lse, "lse", torch.float32, dev, (nq, H))
     if ws is None:
         ws = _made(stream, workspace, lib.dsa_sparse_mla_workspace_size(batch.c, H, k), dev)
-    _check(_ATTN[dt](pq, pr, pkv, kv.shape[0], pi, k, H, float(scale), batch._ref, po,
-                     None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
+    pw, wn = _ws(ws, dev)
+    _check(_ATTN[dt](pq, pr, pkv, kv.shape[0], pi, k, H, float(scale), batch._ref, po, pl, pw, wn,
                      _raw_stream(stream, dev)), "dsa_sparse_mla_attn")
     return out, lse
 
@@ -730,18 +744,20 @@ def dsa_sparse_mla_attn_rows(q_lat, q_rope, kv, rows, batch: Batch, *, scale: fl
     _need(q_rope, "q_rope", torch.bfloat16, dev, (batch.num_q, H, ROPE))
     _need(kv, "kv", (torch.bfloat16, torch.uint8), dev)
     dt = _kv_dtype(kv)
-    _need(rows, "rows", torch.int32, dev)
-    k = rows.shape[1]
+    pi, k = _index_list(rows, "rows", batch.num_q, dev)
     if out is None:
         out = torch.empty((batch.num_q, H, LATENT), dtype=torch.bfloat16, device=dev)
+    _need(out, "out", torch.bfloat16, dev, (batch.num_q, H, LATENT))
     if lse is None and with_lse:
         lse = torch.empty((batch.num_q, H), dtype=torch.float32, device=dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, dev, (batch.num_q, H))
     if ws is None:
         ws = workspace(lib.dsa_sparse_mla_workspace_size(batch.c, H, k), dev)
+    pw, wn = _ws(ws, dev)
     _check(lib.dsa_sparse_mla_attn_rows(_ptr(q_lat), _ptr(q_rope), _ptr(kv), kv.shape[0],
-                                        dt, _ptr(rows), k, H,
-                                        float(scale), batch.c, _ptr(out), _ptr(lse), _ptr(ws),
-                                        ws.numel(), _stream(stream, dev)), "dsa_sparse_mla_attn_rows")
+                                        dt, pi, k, H, float(scale), batch.c, _ptr(out), _ptr(lse),
+                                        pw, wn, _stream(stream, dev)), "dsa_sparse_mla_attn_rows")
     return out, lse
 
 
