@@ -343,10 +343,10 @@ def dsa_indexer_scores(q_idx, w, k_idx, batch: Batch, scores=None, *, q_scale=No
         _need(q_scale, "q_scale", torch.float32, dev, (batch.num_q, INDEX_HEADS))
         _need(k_scale, "k_scale", torch.float32, dev, (k_idx.shape[0],))
     if scores is None:
-        scores = torch.empty((batch.num_q, batch.max_len), dtype=torch.float32, device=dev)
+        scores = _made(stream, torch.empty, (batch.num_q, batch.max_len), dtype=torch.float32, device=dev)
     _need(scores, "scores", torch.float32, dev, (batch.num_q, batch.max_len))
     if ws is None:
-        ws = workspace(lib.dsa_indexer_workspace_size(batch.c), dev)
+        ws = _made(stream, workspace, lib.dsa_indexer_workspace_size(batch.c), dev)
     _check(lib.dsa_indexer_scores(_ptr(q_idx), _ptr(q_scale), _ptr(w), _ptr(k_idx), _ptr(k_scale),
                                   k_idx.shape[0], dt, batch.c, _ptr(scores), _ptr(ws), ws.numel(),
                                   _stream(stream, dev)), "dsa_indexer_scores")
@@ -358,10 +358,10 @@ def dsa_topk(scores, batch: Batch, k: int, idx=None, *, ws=None, stream=None):
     dev = batch.device
     _need(scores, "scores", torch.float32, dev, (batch.num_q, batch.max_len))
     if idx is None:
-        idx = torch.empty((batch.num_q, k), dtype=torch.int32, device=dev)
+        idx = _made(stream, torch.empty, (batch.num_q, k), dtype=torch.int32, device=dev)
     _need(idx, "idx", torch.int32, dev, (batch.num_q, k))
     if ws is None:
-        ws = workspace(lib.dsa_topk_workspace_size(batch.c, k), dev)
+        ws = _made(stream, workspace, lib.dsa_topk_workspace_size(batch.c, k), dev)
     _check(lib.dsa_topk(_ptr(scores), batch.c, k, _ptr(idx), _ptr(ws), ws.numel(),
                         _stream(stream, dev)), "dsa_topk")
     return idx
@@ -404,7 +404,7 @@ def dsa_kv_fp8_quantize(kv, out=None, *, stream=None):
     if kv.dim() != 2 or kv.shape[1] != KV_ROW:
         raise ValueError("kv must be [rows, 576]")
     if out is None:
-        out = torch.empty((kv.shape[0], KV_ROW_FP8), dtype=torch.uint8, device=kv.device)
+        out = _made(stream, torch.empty, (kv.shape[0], KV_ROW_FP8), dtype=torch.uint8, device=kv.device)
     _need(out, "out", torch.uint8, kv.device, (kv.shape[0], KV_ROW_FP8))
     _check(lib.dsa_kv_fp8_quantize(_ptr(kv), kv.shape[0], _ptr(out), _stream(stream, kv.device)),
            "dsa_kv_fp8_quantize")
@@ -549,10 +549,10 @@ def indexshare_group_forward(group: Group, batch: Batch, idx_buf=None, *, ws=Non
     indices."""
     dev = batch.device
     if idx_buf is None:
-        idx_buf = torch.empty((batch.num_q, group.k), dtype=torch.int32, device=dev)
+        idx_buf = _made(stream, torch.empty, (batch.num_q, group.k), dtype=torch.int32, device=dev)
     _need(idx_buf, "idx_buf", torch.int32, dev, (batch.num_q, group.k))
     if ws is None:
-        ws = workspace(group.workspace_size(batch), dev)
+        ws = _made(stream, workspace, group.workspace_size(batch), dev)
     _check(lib.indexshare_group_forward(group.c, batch.c, _ptr(idx_buf), _ptr(ws), ws.numel(),
                                         _stream(stream, dev)), "indexshare_group_forward")
     return group.outs, group.lses, idx_buf
@@ -566,9 +566,9 @@ def dsa_fp8_quantize(x, codes=None, scale=None, *, stream=None):
         raise ValueError("last dimension must be 128")
     rows = x.numel() // 128
     if codes is None:
-        codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        codes = _made(stream, torch.empty, x.shape, dtype=torch.uint8, device=x.device)
     if scale is None:
-        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        scale = _made(stream, torch.empty, x.shape[:-1], dtype=torch.float32, device=x.device)
     _need(codes, "codes", torch.uint8, x.device)
     _need(scale, "scale", torch.float32, x.device)
     _check(lib.dsa_fp8_quantize(_ptr(x), rows, _ptr(codes), _ptr(scale), _stream(stream, x.device)),
@@ -604,7 +604,7 @@ def dsa_indexer_append_keys(k_new, k_seq, k_pos, batch: Batch, k_cache, inv_freq
     if fp8:
         _need(k_scale, "k_scale", torch.float32, dev, (k_cache.shape[0],))
     if ws is None:
-        ws = workspace(STATUS_BYTES, dev)
+        ws = _made(stream, workspace, STATUS_BYTES, dev)
     _check(lib.dsa_indexer_append_keys(_ptr(k_new), _ptr(k_seq), _ptr(k_pos), n, batch.c,
                                        DSA_FP8_E4M3 if fp8 else DSA_BF16, _freq(inv_freq),
                                        _ptr(k_cache), _ptr(k_scale) if fp8 else None,
@@ -621,12 +621,13 @@ def dsa_indexer_prepare_queries(q_new, batch: Batch, inv_freq, *, fp8=False, q_o
     dev = batch.device
     _need(q_new, "q_new", torch.bfloat16, dev, (batch.num_q, INDEX_HEADS, INDEX_DIM))
     if q_out is None:
-        q_out = torch.empty(q_new.shape, dtype=torch.uint8 if fp8 else torch.bfloat16, device=dev)
+        q_out = _made(stream, torch.empty, q_new.shape, dtype=torch.uint8 if fp8 else torch.bfloat16,
+                      device=dev)
     if fp8 and q_scale is None:
-        q_scale = torch.empty((batch.num_q, INDEX_HEADS), dtype=torch.float32, device=dev)
+        q_scale = _made(stream, torch.empty, (batch.num_q, INDEX_HEADS), dtype=torch.float32, device=dev)
     _need(q_out, "q_out", torch.uint8 if fp8 else torch.bfloat16, dev, tuple(q_new.shape))
     if ws is None:
-        ws = workspace(STATUS_BYTES, dev)
+        ws = _made(stream, workspace, STATUS_BYTES, dev)
     _check(lib.dsa_indexer_prepare_queries(_ptr(q_new), batch.c, DSA_FP8_E4M3 if fp8 else DSA_BF16,
                                            _freq(inv_freq), _ptr(q_out),
                                            _ptr(q_scale) if fp8 else None, _ptr(ws), ws.numel(),
@@ -683,10 +684,10 @@ def dsa_hot_plan(idx, batch: Batch, state: HotState, step: int, rows=None, *, ws
     _need(idx, "idx", torch.int32, dev)
     k = idx.shape[1]
     if rows is None:
-        rows = torch.empty((batch.num_q, k), dtype=torch.int32, device=dev)
+        rows = _made(stream, torch.empty, (batch.num_q, k), dtype=torch.int32, device=dev)
     _need(rows, "rows", torch.int32, dev, (batch.num_q, k))
     if ws is None:
-        ws = workspace(STATUS_BYTES, dev)
+        ws = _made(stream, workspace, STATUS_BYTES, dev)
     _check(lib.dsa_hot_plan(_ptr(idx), k, batch.c, state.c, int(step), _ptr(rows), _ptr(ws),
                             ws.numel(), _stream(stream, dev)), "dsa_hot_plan")
     return rows
@@ -709,7 +710,7 @@ def dsa_hot_fetch(state: HotState, batch: Batch, cold_kv, hot_kv, *, ws=None, st
         if cold_kv[l].dtype != cold_kv[0].dtype or tuple(cold_kv[l].shape) != tuple(cold_kv[0].shape):
             raise ValueError("cold caches must share dtype and shape")
     if ws is None:
-        ws = workspace(STATUS_BYTES, dev)
+        ws = _made(stream, workspace, STATUS_BYTES, dev)
     cold = (c_void_p * n)(*[t.data_ptr() for t in cold_kv])
     hot = (c_void_p * n)(*[t.data_ptr() for t in hot_kv])
     _check(lib.dsa_hot_fetch(state.c, batch.c, n, ctypes.cast(cold, _PP), cold_kv[0].shape[0],
@@ -746,14 +747,14 @@ def dsa_sparse_mla_attn_rows(q_lat, q_rope, kv, rows, batch: Batch, *, scale: fl
     dt = _kv_dtype(kv)
     pi, k = _index_list(rows, "rows", batch.num_q, dev)
     if out is None:
-        out = torch.empty((batch.num_q, H, LATENT), dtype=torch.bfloat16, device=dev)
+        out = _made(stream, torch.empty, (batch.num_q, H, LATENT), dtype=torch.bfloat16, device=dev)
     _need(out, "out", torch.bfloat16, dev, (batch.num_q, H, LATENT))
     if lse is None and with_lse:
-        lse = torch.empty((batch.num_q, H), dtype=torch.float32, device=dev)
+        lse = _made(stream, torch.empty, (batch.num_q, H), dtype=torch.float32, device=dev)
     if lse is not None:
         _need(lse, "lse", torch.float32, dev, (batch.num_q, H))
     if ws is None:
-        ws = workspace(lib.dsa_sparse_mla_workspace_size(batch.c, H, k), dev)
+        ws = _made(stream, workspace, lib.dsa_sparse_mla_workspace_size(batch.c, H, k), dev)
     pw, wn = _ws(ws, dev)
     _check(lib.dsa_sparse_mla_attn_rows(_ptr(q_lat), _ptr(q_rope), _ptr(kv), kv.shape[0],
                                         dt, pi, k, H, float(scale), batch.c, _ptr(out), _ptr(lse),
@@ -795,11 +796,11 @@ def indexshare_group_forward_hot(group: Group, batch: Batch, hot: HotGroup, step
         if hk.dtype != ck.dtype or hk.shape[1] != ck.shape[1]:
             raise ValueError(f"layer {l}: hot and cold rows differ in dtype or width")
     if idx_buf is None:
-        idx_buf = torch.empty((batch.num_q, group.k), dtype=torch.int32, device=dev)
+        idx_buf = _made(stream, torch.empty, (batch.num_q, group.k), dtype=torch.int32, device=dev)
     _need(idx_buf, "idx_buf", torch.int32, dev, (batch.num_q, group.k))
     _need(hot.rows, "hot.rows", torch.int32, dev, (batch.num_q, group.k))
     if ws is None:
-        ws = workspace(group.workspace_size(batch), dev)
+        ws = _made(stream, workspace, group.workspace_size(batch), dev)
     hot._c.step = int(step)
     _check(lib.indexshare_group_forward_hot(group.c, batch.c, ctypes.byref(hot._c), _ptr(idx_buf),
                                             _ptr(ws), ws.numel(), _stream(stream, dev)),

@@ -93,3 +93,86 @@ def test_attention_refuses_a_workspace_that_is_none(dsa, name):
     with pytest.raises(TypeError):
         _attention(name, dsa, ws=4096)
     assert not dsa.reached
+
+
+# ---------------------------------------------------------------- memory of the given stream
+I32, F32, U8 = torch.int32, torch.float32, torch.uint8
+
+
+def _state():
+    return SimpleNamespace(c=None, _c=None, num_seqs=1, hot_slots=8, max_pos=128)
+
+
+def _group():
+    return SimpleNamespace(k=K, c=None, outs=[], lses=None, layer_types="F", layers=[dict(kv=gpu(64, 576))],
+                           workspace_size=lambda batch: 256)
+
+
+def _hot(m):
+    return SimpleNamespace(cold_kv=[gpu(64, 576)], spans=[_state()], rows=gpu(NQ, K, dtype=I32),
+                           _c=m._HotGroup())
+
+
+def _entries():
+    return gpu(NQ, dtype=I32), gpu(NQ, dtype=I32)
+
+
+# every entry point that makes an output or a workspace where the caller gives none
+CALLS = {
+    "dsa_indexer_scores": lambda m, s: m.dsa_indexer_scores(
+        gpu(NQ, 32, 128), gpu(NQ, 32, dtype=F32), gpu(64, 128), _batch(), stream=s),
+    "dsa_topk": lambda m, s: m.dsa_topk(gpu(NQ, 128, dtype=F32), _batch(), K, stream=s),
+    "dsa_sparse_mla_attn": lambda m, s: m.dsa_sparse_mla_attn(
+        gpu(NQ, H, 512), gpu(NQ, H, 64), gpu(64, 576), gpu(NQ, K, dtype=I32), _batch(), scale=1.0, stream=s),
+    "dsa_sparse_mla_attn_rows": lambda m, s: m.dsa_sparse_mla_attn_rows(
+        gpu(NQ, H, 512), gpu(NQ, H, 64), gpu(64, 576), gpu(NQ, K, dtype=I32), _batch(), scale=1.0, stream=s),
+    "dsa_kv_fp8_quantize": lambda m, s: m.dsa_kv_fp8_quantize(gpu(NQ, 576), stream=s),
+    "dsa_kv_int4_quantize": lambda m, s: m.dsa_kv_int4_quantize(gpu(NQ, 576), stream=s),
+    "dsa_kv_append": lambda m, s: m.dsa_kv_append(gpu(NQ, 576), *_entries(), _batch(), gpu(64, 576), stream=s),
+    "dsa_kv_read": lambda m, s: m.dsa_kv_read(gpu(64, 576), *_entries(), _batch(), stream=s),
+    "dsa_fp8_quantize": lambda m, s: m.dsa_fp8_quantize(gpu(NQ, 128), stream=s),
+    "dsa_indexer_append_keys": lambda m, s: m.dsa_indexer_append_keys(
+        gpu(NQ, 128), *_entries(), _batch(), gpu(64, 128), [0.5] * 32, stream=s),
+    "dsa_indexer_prepare_queries": lambda m, s: m.dsa_indexer_prepare_queries(
+        gpu(NQ, 32, 128), _batch(), [0.5] * 32, fp8=True, stream=s),
+    "dsa_hot_plan": lambda m, s: m.dsa_hot_plan(gpu(NQ, K, dtype=I32), _batch(), _state(), 0, stream=s),
+    "dsa_hot_fetch": lambda m, s: m.dsa_hot_fetch(_state(), _batch(), [gpu(64, 576)], [gpu(8, 576)], stream=s),
+    "indexshare_group_forward": lambda m, s: m.indexshare_group_forward(_group(), _batch(), stream=s),
+    "indexshare_group_forward_hot": lambda m, s: m.indexshare_group_forward_hot(
+        _group(), _batch(), _hot(m), 0, stream=s),
+}
+
+
+class _TorchThatMakesNothing:
+    """torch, whose makers of tensors must not be reached past _made."""
+
+    def __getattr__(self, name):
+        if name in ("empty", "zeros", "full"):
+            def make(*a, **k):
+                raise AssertionError(f"torch.{name} on the current stream")
+            return make
+        return getattr(torch, name)
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_a_call_makes_its_tensors_on_the_stream_that_it_works_on(dsa, monkeypatch, name):
+    m, made = dsa.m, []
+    space = m.workspace
+
+    def record(stream, make, *args, **kw):
+        made.append(stream)
+        return gpu(4096, dtype=U8) if make is space else gpu(*args[0], dtype=kw["dtype"])
+
+    monkeypatch.setattr(m, "_made", record)
+    monkeypatch.setattr(m, "torch", _TorchThatMakesNothing())
+    CALLS[name](m, STREAM)
+    assert made and all(s is STREAM for s in made) and dsa.reached
+
+
+def test_every_entry_point_with_a_stream_is_listed(dsa):
+    import inspect
+
+    names = {n for n, f in vars(dsa.m).items() if inspect.isfunction(f) and not n.startswith("_")
+             and "stream" in inspect.signature(f).parameters}
+    # these make nothing: the status of a given workspace, a self-test over one, reads of host pages
+    assert names == set(CALLS) | {"status_fetch", "dsa_selftest_wait_timeout", "dsa_hot_touch"}
