@@ -25,7 +25,7 @@
 // the read-back the other way round.  Measured (times in a graph): the read-back of
 // 131,072 INT4 rows in 32.4 us, 6.36 TB/s or 0.95 of the copy rate; of 16,301 INT4
 // rows in 5.4 us and 27,009 FP8 rows in 6.6 us (in L2).  The append of 4096 INT4 rows
-// takes 4.6 us, of 4503 FP8 rows 5.6 us, of one row 2.5 us: two thirds are the
+// takes 4.6 us, of 4503 FP8 rows 5.7 us, of one row 2.5 us: two thirds are the
 // launch and the chain of a row (its place, its values, the group's maximum, the
 // codes), as 4096 rows are seven warps a scheduler.
 #include <cmath>
@@ -105,8 +105,9 @@ __device__ __forceinline__ uint32_t int4_word(const uint4& w, uint16_t& scale_bi
 }
 
 // Eight E4M3 codes and their group's scale; the group is 16 lanes.  The scale is
-// amax * fp32(1/448), within one unit in the last place of amax / 448: one
-// product in place of a division per lane.  A code is the E4M3 value nearest to
+// the fp32 nearest to amax / 448, as in every FP8 row (kv_fp8_quant_kernel): a
+// cache may hold rows of both calls.  (The product amax * fp32(1/448) would be an ulp off
+// in six groups of ten; 4503 rows take 5.59 us with it and 5.71 with the division.)  A code is the E4M3 value nearest to
 // the exact x / sc (one element in 200 of a random group is an exact midpoint, so
 // it is decided for all): q = |x| * (1/sc) gives the interval between two codes,
 // m is its midpoint, the sign of the fma |x| - m sc is that of |x| / sc - m
@@ -123,7 +124,7 @@ __device__ __forceinline__ uint2 fp8_codes8(const uint4& w, float& sc) {
   for (int d = 0; d < 8; ++d) amax = fmaxf(amax, fabsf(v[d]));
 #pragma unroll
   for (int m = 1; m < 16; m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-  sc = amax > 0.f ? __fmul_rn(amax, 1.f / 448.f) : 1.f;
+  sc = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
   const float r = rcp_approx(sc);
   uint32_t o[4];
 #pragma unroll

@@ -401,11 +401,9 @@ DSA_API dsa_status_t dsa_sparse_mla_attn_int4kv(const void* q_lat, const void* q
  * by kv_pos * inv_freq[i], the fp64 rotation rounded once to bf16; inv_freq: 32
  * finite host doubles, or NULL where the keys come already rotated), and the row is
  * written in the cache's format (kv_dtype DSA_BF16, DSA_FP8_E4M3 or DSA_INT4) at the
- * position's place in the batch layout (contiguous or paged).  INT4 rows are those of
- * dsa_kv_int4_quantize bit for bit.  FP8 rows have the layout and the codes (nearest
- * E4M3 to the exact x / scale) of dsa_kv_fp8_quantize with the scale amax * fp32(1/448),
- * one fp32 product: it is within one unit in the last place of that call's amax / 448,
- * so a code can differ from that call's where x / scale lies on a midpoint.
+ * position's place in the batch layout (contiguous or paged).  FP8 and INT4 rows are
+ * those of dsa_kv_fp8_quantize and dsa_kv_int4_quantize of the rotated row, bit for
+ * bit, so a cache may be converted in part and appended to.
  *
  * dsa_kv_read: out[i] (bf16 [n, 576]) = the values that the cache row of entry i
  * stands for, in bf16 (what the attention reads).

@@ -262,27 +262,7 @@ def kv_append_rows(kv_bf16_bits, pos, inv_freq, kind):
     kv = np.array(np.asarray(kv_bf16_bits, np.uint16).reshape(-1, 576))
     if inv_freq is not None and len(kv):
         kv[:, 512:] = rope_bf16(kv[:, 512:], pos, inv_freq, 64)
-    return {"bf16": lambda r: r, "fp8": _kv_fp8_append_rows, "int4": kv_int4_quantize}[kind](kv)
-
-
-def _kv_fp8_append_rows(bits):
-    """FP8 rows as the append writes them: those of kv_fp8_quantize with the scale
-    amax * fp32(1/448), one fp32 product."""
-    n = bits.shape[0]
-    x = _bf16_f64(bits[:, :512]).reshape(n, 4, 128)
-    amax = np.abs(x).max(axis=2).astype(np.float32)
-    s = np.where(amax > 0, amax * np.float32(1 / 448), np.float32(1)).astype(np.float32)
-    q = np.abs(x) / s.astype(np.float64)[:, :, None]
-    step = np.ldexp(1.0, np.maximum(np.frexp(q)[1], -5) - 4)
-    q = np.minimum(np.rint(q / step) * step, 448.0)
-    grid = e4m3_decode(np.arange(127, dtype=np.uint8)).astype(np.float64)  # 0 .. 448, ascending
-    code = np.searchsorted(grid, q)
-    assert np.array_equal(grid[code], q)
-    out = np.empty((n, 656), np.uint8)
-    out[:, :512] = (code + 128 * np.signbit(x)).astype(np.uint8).reshape(n, 512)
-    out[:, 512:528] = s.view(np.uint8).reshape(n, 16)
-    out[:, 528:] = np.ascontiguousarray(bits[:, 512:]).view(np.uint8)
-    return out
+    return {"bf16": lambda r: r, "fp8": kv_fp8_quantize, "int4": kv_int4_quantize}[kind](kv)
 
 
 # ---------------------------------------------------------------- batch helpers
