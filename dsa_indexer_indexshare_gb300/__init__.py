@@ -258,6 +258,14 @@ def _made(stream, make, *args, **kw):
     return make(*args, **kw)
 
 
+def _capturing(stream):
+    """Whether the stream that a call works on is being captured into a graph."""
+    if isinstance(stream, torch.cuda.Stream):
+        with torch.cuda.stream(stream):
+            return torch.cuda.is_current_stream_capturing()
+    return torch.cuda.is_current_stream_capturing()
+
+
 def status_fetch(ws: torch.Tensor, stream=None):
     """Synchronise, read and clear the device status of a workspace; raise on error."""
     bits = c_int32(0)
@@ -431,7 +439,10 @@ def dsa_kv_append(kv_new, kv_seq, kv_pos, batch: Batch, kv, inv_freq=None, *, ws
     entry i at position kv_pos[i] of sequence kv_seq[i] (int32 [n], -1: padding).
     The keys are rotated by the 32 frequencies inv_freq (host sequence; None: they
     come rotated), the rows quantised to kv's row type (bf16 [rows, 576], FP8 uint8
-    [rows, 656], INT4 uint8 [rows, 416]).  Returns kv."""
+    [rows, 656], INT4 uint8 [rows, 416]).  Returns kv.  An entry outside the batch or
+    the cache is left out and reported: in ws (status_fetch), or, where none is given,
+    by this call, which then waits for its kernel and raises (but cannot in a graph's
+    capture: give a ws there)."""
     dev = batch.device
     if not isinstance(kv_new, torch.Tensor):
         raise TypeError("kv_new must be a tensor")
@@ -449,11 +460,14 @@ def dsa_kv_append(kv_new, kv_seq, kv_pos, batch: Batch, kv, inv_freq=None, *, ws
     pp = _addr(kv_pos, "kv_pos", torch.int32, dev, (n,))
     dt = _kv_dtype(kv)
     pkv = _addr(kv, "kv", kv.dtype, dev, kv.shape)
-    if ws is None:
+    report = ws is None
+    if report:
         ws = _made(stream, workspace, STATUS_BYTES, dev)
     _check(lib.dsa_kv_append(kv_new.data_ptr(), stride, ps, pp, n, batch._ref, dt,
                              None if inv_freq is None else _freq(inv_freq), pkv, kv.shape[0],
                              ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)), "dsa_kv_append")
+    if report and not _capturing(stream):  # a row that is not written is lost to every later step
+        status_fetch(ws, stream)
     return kv
 
 

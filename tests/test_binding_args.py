@@ -35,6 +35,7 @@ def dsa(monkeypatch):
 
     fake = Lib()
     monkeypatch.setattr(m, "lib", fake)
+    monkeypatch.setattr(m, "_capturing", lambda stream: False, raising=False)
     monkeypatch.setattr(m, "_ATTN", {t: fake.attention for t in m._ATTN})
     return SimpleNamespace(m=m, reached=reached)
 
@@ -176,3 +177,16 @@ def test_every_entry_point_with_a_stream_is_listed(dsa):
              and "stream" in inspect.signature(f).parameters}
     # these make nothing: the status of a given workspace, a self-test over one, reads of host pages
     assert names == set(CALLS) | {"status_fetch", "dsa_selftest_wait_timeout", "dsa_hot_touch"}
+
+
+# ---------------------------------------------------------------- rows that are not written
+@pytest.mark.parametrize("given,capturing,fetched", [(False, False, 1), (False, True, 0), (True, False, 0)])
+def test_append_without_a_workspace_reports_its_entries(dsa, monkeypatch, given, capturing, fetched):
+    m, seen = dsa.m, []
+    monkeypatch.setattr(m, "_made", lambda stream, make, *a, **k: gpu(4096, dtype=U8))
+    monkeypatch.setattr(m, "_capturing", lambda stream: capturing)
+    monkeypatch.setattr(m, "status_fetch", lambda ws, stream=None: seen.append((ws, stream)))
+    ws = gpu(4096, dtype=U8) if given else None
+    m.dsa_kv_append(gpu(NQ, 576), *_entries(), _batch(), gpu(64, 576), ws=ws, stream=STREAM)
+    assert dsa.reached == ["dsa_kv_append"] and len(seen) == fetched
+    assert all(s is STREAM for _, s in seen)
