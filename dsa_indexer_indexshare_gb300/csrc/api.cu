@@ -129,6 +129,9 @@ dsa_status_t check_mla_args(const void* q_lat, const void* q_rope, const void* k
   if (kv_rows < 1 || kv_rows > (int64_t(1) << 31) - 1)
     return fail(DSA_ERR_INVALID_ARG, "kv_rows=%lld", static_cast<long long>(kv_rows));
   if (!(scale == scale)) return fail(DSA_ERR_INVALID_ARG, "scale is NaN");
+  // (the INT4 kernels hold the scores times 2^-40: 2^40 * log2(e) * scale has to be finite)
+  if (dt == DSA_INT4 && !(std::fabs(scale) < 0x1p87f))
+    return fail(DSA_ERR_UNSUPPORTED, "scale=%g (supported over INT4 rows: below 2^87)", scale);
   if (static_cast<int64_t>(b->num_q) * heads > (int64_t(1) << 31) - 1)
     return fail(DSA_ERR_UNSUPPORTED, "num_q * heads >= 2^31");
   return DSA_OK;

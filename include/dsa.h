@@ -378,8 +378,8 @@ DSA_API dsa_status_t dsa_sparse_mla_attn_fp8kv(const void* q_lat, const void* q_
  * [kv_rows, 416], heads 16, 32 or 64).  The attention is the bf16 one on the values
  * above, and a key that is not read (a -1 entry, a position that is not visible or
  * has no row) adds nothing whatever the cache holds.  (Inside, values and RoPE
- * keys are held times 2^-40: those below 2^-86 lose bits, and |scale| must stay
- * below 2^87.)  The group calls take such caches with dsa_group_t.kv_dtype = DSA_INT4, dsa_sparse_mla_attn_rows and the
+ * keys are held times 2^-40: those below 2^-86 lose bits, and a |scale| of 2^87 or
+ * more returns DSA_ERR_UNSUPPORTED.)  The group calls take such caches with dsa_group_t.kv_dtype = DSA_INT4, dsa_sparse_mla_attn_rows and the
  * hot buffer with kv_dtype = DSA_INT4.
  */
 DSA_API dsa_status_t dsa_kv_int4_quantize(const void* kv, int64_t rows, uint8_t* out,
