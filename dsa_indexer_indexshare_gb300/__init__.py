@@ -179,9 +179,10 @@ def _need(t, name, dtype=None, device=None, shape=None):
 
 def _addr(t, name, dtype, device, shape):
     """Address of a tensor that _need accepts; the common case is checked here,
-    without _need's calls (a decode step is a few microseconds of kernels)."""
-    if not (type(t) is torch.Tensor and t.dtype is dtype and t.device == device and t.shape == shape
-            and t.is_contiguous() and t.is_cuda):
+    without _need's calls (a decode step is a few microseconds of kernels).  Host
+    tensors have device number -1."""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == device.index
+            and t.shape == shape and t.is_contiguous()):
         _need(t, name, dtype, device, shape)
     return t.data_ptr()
 
@@ -190,7 +191,7 @@ def _ws(ws, device):
     """Address and size of a workspace that the caller gives."""
     if not isinstance(ws, torch.Tensor):
         raise TypeError("ws must be a tensor")
-    if not (ws.is_cuda and ws.device == device and ws.is_contiguous()):
+    if not (ws.get_device() == device.index and ws.is_contiguous()):
         raise ValueError(f"ws must be a contiguous tensor on {device}")
     return ws.data_ptr(), ws.numel()
 
@@ -218,6 +219,8 @@ class Batch:
         self.max_q = int(np.diff(qs).max(initial=0)) if qs.size > 1 else 0
         self.max_len = int(max_len)
         dev = torch.device(device)
+        if dev.type != "cuda":
+            dev = torch.device(dev.type)  # no device number: that of a GPU is what the calls compare
         self.device = dev
         self.q_start = torch.as_tensor(np.asarray(q_start, np.int32), device=dev)
         self.q_pos = torch.as_tensor(np.asarray(q_pos, np.int32), device=dev)
@@ -356,7 +359,7 @@ def dsa_indexer_scores(q_idx, w, k_idx, batch: Batch, scores=None, *, q_scale=No
     if ws is None:
         ws = _made(stream, workspace, lib.dsa_indexer_workspace_size(batch.c), dev)
     _check(lib.dsa_indexer_scores(_ptr(q_idx), _ptr(q_scale), _ptr(w), _ptr(k_idx), _ptr(k_scale),
-                                  k_idx.shape[0], dt, batch.c, _ptr(scores), _ptr(ws), ws.numel(),
+                                  k_idx.shape[0], dt, batch.c, _ptr(scores), *_ws(ws, dev),
                                   _stream(stream, dev)), "dsa_indexer_scores")
     return scores
 
@@ -370,7 +373,7 @@ def dsa_topk(scores, batch: Batch, k: int, idx=None, *, ws=None, stream=None):
     _need(idx, "idx", torch.int32, dev, (batch.num_q, k))
     if ws is None:
         ws = _made(stream, workspace, lib.dsa_topk_workspace_size(batch.c, k), dev)
-    _check(lib.dsa_topk(_ptr(scores), batch.c, k, _ptr(idx), _ptr(ws), ws.numel(),
+    _check(lib.dsa_topk(_ptr(scores), batch.c, k, _ptr(idx), *_ws(ws, dev),
                         _stream(stream, dev)), "dsa_topk")
     return idx
 
@@ -395,8 +398,7 @@ def dsa_sparse_mla_attn(q_lat, q_rope, kv, idx, batch: Batch, *, scale: float, o
     pl = None if lse is None else _addr(lse, "lse", torch.float32, dev, (nq, H))
     if ws is None:
         ws = _made(stream, workspace, lib.dsa_sparse_mla_workspace_size(batch.c, H, k), dev)
-    pw, wn = _ws(ws, dev)
-    _check(_ATTN[dt](pq, pr, pkv, kv.shape[0], pi, k, H, float(scale), batch._ref, po, pl, pw, wn,
+    _check(_ATTN[dt](pq, pr, pkv, kv.shape[0], pi, k, H, float(scale), batch._ref, po, pl, *_ws(ws, dev),
                      _raw_stream(stream, dev)), "dsa_sparse_mla_attn")
     return out, lse
 
@@ -465,7 +467,7 @@ def dsa_kv_append(kv_new, kv_seq, kv_pos, batch: Batch, kv, inv_freq=None, *, ws
         ws = _made(stream, workspace, STATUS_BYTES, dev)
     _check(lib.dsa_kv_append(kv_new.data_ptr(), stride, ps, pp, n, batch._ref, dt,
                              None if inv_freq is None else _freq(inv_freq), pkv, kv.shape[0],
-                             ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)), "dsa_kv_append")
+                             *_ws(ws, dev), _raw_stream(stream, dev)), "dsa_kv_append")
     if report and not _capturing(stream):  # a row that is not written is lost to every later step
         status_fetch(ws, stream)
     return kv
@@ -485,7 +487,7 @@ def dsa_kv_read(kv, kv_seq, kv_pos, batch: Batch, out=None, *, ws=None, stream=N
     po = _addr(out, "out", torch.bfloat16, dev, (n, KV_ROW))
     if ws is None:
         ws = _made(stream, workspace, STATUS_BYTES, dev)
-    _check(lib.dsa_kv_read(pkv, kv.shape[0], dt, ps, pp, n, batch._ref, po, ws.data_ptr(), ws.numel(),
+    _check(lib.dsa_kv_read(pkv, kv.shape[0], dt, ps, pp, n, batch._ref, po, *_ws(ws, dev),
                            _raw_stream(stream, dev)), "dsa_kv_read")
     return out
 
@@ -521,8 +523,14 @@ class Group:
                 if self.idx_dtype == DSA_FP8_E4M3:
                     _need(L["q_scale"], f"q_scale[{l}]", torch.float32, dev, (num_q, INDEX_HEADS))
                     _need(L["k_scale"], f"k_scale[{l}]", torch.float32, dev)
+                    if L["k_scale"].numel() < L["k_idx"].shape[0]:
+                        raise ValueError(f"k_scale[{l}] must hold a scale per row of k_idx")
         self.outs = outs if outs is not None else [
             torch.empty((num_q, H, LATENT), dtype=torch.bfloat16, device=dev) for _ in range(nl)]
+        if len(self.outs) != nl:
+            raise ValueError("one output per layer")
+        for l, o in enumerate(self.outs):
+            _need(o, f"outs[{l}]", torch.bfloat16, dev, (num_q, H, LATENT))
         self.lses = [torch.empty((num_q, H), dtype=torch.float32, device=dev)
                      for _ in range(nl)] if with_lse else None
 
@@ -557,17 +565,23 @@ class Group:
         return lib.dsa_group_workspace_size(self.c, batch.c)
 
 
+def _holds(group, batch):
+    if group.num_q < batch.num_q:
+        raise ValueError(f"group of {group.num_q} queries for a batch of {batch.num_q}")
+
+
 def indexshare_group_forward(group: Group, batch: Batch, idx_buf=None, *, ws=None, stream=None):
     """Run one layer group; returns (outs, lses, idx_buf).  outs[l] is the
     layer's [num_q, H, 512] bf16 output; idx_buf holds the last F layer's
     indices."""
     dev = batch.device
+    _holds(group, batch)
     if idx_buf is None:
         idx_buf = _made(stream, torch.empty, (batch.num_q, group.k), dtype=torch.int32, device=dev)
     _need(idx_buf, "idx_buf", torch.int32, dev, (batch.num_q, group.k))
     if ws is None:
         ws = _made(stream, workspace, group.workspace_size(batch), dev)
-    _check(lib.indexshare_group_forward(group.c, batch.c, _ptr(idx_buf), _ptr(ws), ws.numel(),
+    _check(lib.indexshare_group_forward(group.c, batch.c, _ptr(idx_buf), *_ws(ws, dev),
                                         _stream(stream, dev)), "indexshare_group_forward")
     return group.outs, group.lses, idx_buf
 
@@ -585,6 +599,8 @@ def dsa_fp8_quantize(x, codes=None, scale=None, *, stream=None):
         scale = _made(stream, torch.empty, x.shape[:-1], dtype=torch.float32, device=x.device)
     _need(codes, "codes", torch.uint8, x.device)
     _need(scale, "scale", torch.float32, x.device)
+    if codes.numel() < x.numel() or scale.numel() < rows:
+        raise ValueError(f"codes and scale must hold {x.numel()} and {rows} entries")
     _check(lib.dsa_fp8_quantize(_ptr(x), rows, _ptr(codes), _ptr(scale), _stream(stream, x.device)),
            "dsa_fp8_quantize")
     return codes, scale
@@ -614,6 +630,8 @@ def dsa_indexer_append_keys(k_new, k_seq, k_pos, batch: Batch, k_cache, inv_freq
     _need(k_seq, "k_seq", torch.int32, dev, (n,))
     _need(k_pos, "k_pos", torch.int32, dev, (n,))
     _need(k_cache, "k_cache", (torch.bfloat16, torch.uint8), dev)
+    if k_cache.dim() < 1 or k_cache.numel() < k_cache.shape[0] * INDEX_DIM:
+        raise ValueError("k_cache must be [rows, 128]")
     fp8 = k_cache.dtype == torch.uint8
     if fp8:
         _need(k_scale, "k_scale", torch.float32, dev, (k_cache.shape[0],))
@@ -622,7 +640,7 @@ def dsa_indexer_append_keys(k_new, k_seq, k_pos, batch: Batch, k_cache, inv_freq
     _check(lib.dsa_indexer_append_keys(_ptr(k_new), _ptr(k_seq), _ptr(k_pos), n, batch.c,
                                        DSA_FP8_E4M3 if fp8 else DSA_BF16, _freq(inv_freq),
                                        _ptr(k_cache), _ptr(k_scale) if fp8 else None,
-                                       k_cache.shape[0], _ptr(ws), ws.numel(),
+                                       k_cache.shape[0], *_ws(ws, dev),
                                        _stream(stream, dev)), "dsa_indexer_append_keys")
     return k_cache
 
@@ -640,11 +658,13 @@ def dsa_indexer_prepare_queries(q_new, batch: Batch, inv_freq, *, fp8=False, q_o
     if fp8 and q_scale is None:
         q_scale = _made(stream, torch.empty, (batch.num_q, INDEX_HEADS), dtype=torch.float32, device=dev)
     _need(q_out, "q_out", torch.uint8 if fp8 else torch.bfloat16, dev, tuple(q_new.shape))
+    if fp8:
+        _need(q_scale, "q_scale", torch.float32, dev, (batch.num_q, INDEX_HEADS))
     if ws is None:
         ws = _made(stream, workspace, STATUS_BYTES, dev)
     _check(lib.dsa_indexer_prepare_queries(_ptr(q_new), batch.c, DSA_FP8_E4M3 if fp8 else DSA_BF16,
                                            _freq(inv_freq), _ptr(q_out),
-                                           _ptr(q_scale) if fp8 else None, _ptr(ws), ws.numel(),
+                                           _ptr(q_scale) if fp8 else None, *_ws(ws, dev),
                                            _stream(stream, dev)), "dsa_indexer_prepare_queries")
     return (q_out, q_scale) if fp8 else q_out
 
@@ -690,20 +710,25 @@ class HotState:
         return [list(zip(fp[b, :n[b]].tolist(), fs[b, :n[b]].tolist())) for b in range(self.num_seqs)]
 
 
+def _covers(state, batch):
+    if state.num_seqs < batch.num_seqs:
+        raise ValueError(f"hot state of {state.num_seqs} sequences for a batch of {batch.num_seqs}")
+
+
 def dsa_hot_plan(idx, batch: Batch, state: HotState, step: int, rows=None, *, ws=None, stream=None):
     """One step of the hot buffer: returns rows int32 [num_q, k], the hot row
     of every valid index entry (-1 elsewhere); the state's fetch lists name
     the rows to swap in."""
     dev = batch.device
-    _need(idx, "idx", torch.int32, dev)
-    k = idx.shape[1]
+    _, k = _index_list(idx, "idx", batch.num_q, dev)
+    _covers(state, batch)
     if rows is None:
         rows = _made(stream, torch.empty, (batch.num_q, k), dtype=torch.int32, device=dev)
     _need(rows, "rows", torch.int32, dev, (batch.num_q, k))
     if ws is None:
         ws = _made(stream, workspace, STATUS_BYTES, dev)
-    _check(lib.dsa_hot_plan(_ptr(idx), k, batch.c, state.c, int(step), _ptr(rows), _ptr(ws),
-                            ws.numel(), _stream(stream, dev)), "dsa_hot_plan")
+    _check(lib.dsa_hot_plan(_ptr(idx), k, batch.c, state.c, int(step), _ptr(rows), *_ws(ws, dev),
+                            _stream(stream, dev)), "dsa_hot_plan")
     return rows
 
 
@@ -712,6 +737,7 @@ def dsa_hot_fetch(state: HotState, batch: Batch, cold_kv, hot_kv, *, ws=None, st
     [num_seqs * hot_slots, 576], uint8 [.., 656] or uint8 [.., 416]) from cold_kv[l] (pinned host
     memory, the batch's cache layout)."""
     dev = batch.device
+    _covers(state, batch)
     n = len(cold_kv)
     if len(hot_kv) != n:
         raise ValueError("one hot array per cold cache")
@@ -729,7 +755,7 @@ def dsa_hot_fetch(state: HotState, batch: Batch, cold_kv, hot_kv, *, ws=None, st
     hot = (c_void_p * n)(*[t.data_ptr() for t in hot_kv])
     _check(lib.dsa_hot_fetch(state.c, batch.c, n, ctypes.cast(cold, _PP), cold_kv[0].shape[0],
                              ctypes.cast(hot, _PP), hot_kv[0].shape[0],
-                             dt, _ptr(ws), ws.numel(), _stream(stream, dev)), "dsa_hot_fetch")
+                             dt, *_ws(ws, dev), _stream(stream, dev)), "dsa_hot_fetch")
     return hot_kv
 
 
@@ -769,10 +795,9 @@ def dsa_sparse_mla_attn_rows(q_lat, q_rope, kv, rows, batch: Batch, *, scale: fl
         _need(lse, "lse", torch.float32, dev, (batch.num_q, H))
     if ws is None:
         ws = _made(stream, workspace, lib.dsa_sparse_mla_workspace_size(batch.c, H, k), dev)
-    pw, wn = _ws(ws, dev)
     _check(lib.dsa_sparse_mla_attn_rows(_ptr(q_lat), _ptr(q_rope), _ptr(kv), kv.shape[0],
                                         dt, pi, k, H, float(scale), batch.c, _ptr(out), _ptr(lse),
-                                        pw, wn, _stream(stream, dev)), "dsa_sparse_mla_attn_rows")
+                                        *_ws(ws, dev), _stream(stream, dev)), "dsa_sparse_mla_attn_rows")
     return out, lse
 
 
@@ -786,6 +811,8 @@ class HotGroup:
         self.cold_kv = list(cold_kv)
         for l, t in enumerate(self.cold_kv):
             _cold(t, f"cold_kv[{l}]")
+            if t.dtype != self.cold_kv[0].dtype or t.shape != self.cold_kv[0].shape:
+                raise ValueError("cold caches must share dtype and shape")
         self.rows = torch.empty((num_q, k), dtype=torch.int32, device=device)
         self._spans = (_Hot * len(self.spans))(*[s._c for s in self.spans])
         self._cold = (c_void_p * len(self.cold_kv))(*[t.data_ptr() for t in self.cold_kv])
@@ -800,11 +827,14 @@ def indexshare_group_forward_hot(group: Group, batch: Batch, hot: HotGroup, step
     span's hot buffer, swap in its missing rows for every layer of the span,
     and attend over hot rows.  Returns (outs, lses, idx_buf)."""
     dev = batch.device
+    _holds(group, batch)
     nl = len(group.layer_types)
     if len(hot.cold_kv) != nl:
         raise ValueError(f"{len(hot.cold_kv)} cold caches for {nl} layers")
     if len(hot.spans) != group.layer_types.count("F"):
         raise ValueError("one HotState per F layer")
+    for state in hot.spans:
+        _covers(state, batch)
     for l in range(nl):
         hk, ck = group.layers[l]["kv"], hot.cold_kv[l]
         if hk.dtype != ck.dtype or hk.shape[1] != ck.shape[1]:
@@ -817,6 +847,6 @@ def indexshare_group_forward_hot(group: Group, batch: Batch, hot: HotGroup, step
         ws = _made(stream, workspace, group.workspace_size(batch), dev)
     hot._c.step = int(step)
     _check(lib.indexshare_group_forward_hot(group.c, batch.c, ctypes.byref(hot._c), _ptr(idx_buf),
-                                            _ptr(ws), ws.numel(), _stream(stream, dev)),
+                                            *_ws(ws, dev), _stream(stream, dev)),
            "indexshare_group_forward_hot")
     return group.outs, group.lses, idx_buf

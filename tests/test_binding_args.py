@@ -16,6 +16,9 @@ class OnGpu(torch.Tensor):
     is_cuda = property(lambda t: True)
     device = property(lambda t: DEV)
 
+    def get_device(self):
+        return 0
+
 
 def gpu(*shape, dtype=torch.bfloat16):
     return torch.zeros(shape, dtype=dtype).as_subclass(OnGpu)
@@ -105,7 +108,7 @@ def _state():
 
 
 def _group():
-    return SimpleNamespace(k=K, c=None, outs=[], lses=None, layer_types="F", layers=[dict(kv=gpu(64, 576))],
+    return SimpleNamespace(k=K, c=None, num_q=NQ, outs=[], lses=None, layer_types="F", layers=[dict(kv=gpu(64, 576))],
                            workspace_size=lambda batch: 256)
 
 
@@ -120,27 +123,27 @@ def _entries():
 
 # every entry point that makes an output or a workspace where the caller gives none
 CALLS = {
-    "dsa_indexer_scores": lambda m, s: m.dsa_indexer_scores(
-        gpu(NQ, 32, 128), gpu(NQ, 32, dtype=F32), gpu(64, 128), _batch(), stream=s),
-    "dsa_topk": lambda m, s: m.dsa_topk(gpu(NQ, 128, dtype=F32), _batch(), K, stream=s),
-    "dsa_sparse_mla_attn": lambda m, s: m.dsa_sparse_mla_attn(
-        gpu(NQ, H, 512), gpu(NQ, H, 64), gpu(64, 576), gpu(NQ, K, dtype=I32), _batch(), scale=1.0, stream=s),
-    "dsa_sparse_mla_attn_rows": lambda m, s: m.dsa_sparse_mla_attn_rows(
-        gpu(NQ, H, 512), gpu(NQ, H, 64), gpu(64, 576), gpu(NQ, K, dtype=I32), _batch(), scale=1.0, stream=s),
-    "dsa_kv_fp8_quantize": lambda m, s: m.dsa_kv_fp8_quantize(gpu(NQ, 576), stream=s),
-    "dsa_kv_int4_quantize": lambda m, s: m.dsa_kv_int4_quantize(gpu(NQ, 576), stream=s),
-    "dsa_kv_append": lambda m, s: m.dsa_kv_append(gpu(NQ, 576), *_entries(), _batch(), gpu(64, 576), stream=s),
-    "dsa_kv_read": lambda m, s: m.dsa_kv_read(gpu(64, 576), *_entries(), _batch(), stream=s),
-    "dsa_fp8_quantize": lambda m, s: m.dsa_fp8_quantize(gpu(NQ, 128), stream=s),
-    "dsa_indexer_append_keys": lambda m, s: m.dsa_indexer_append_keys(
-        gpu(NQ, 128), *_entries(), _batch(), gpu(64, 128), [0.5] * 32, stream=s),
-    "dsa_indexer_prepare_queries": lambda m, s: m.dsa_indexer_prepare_queries(
-        gpu(NQ, 32, 128), _batch(), [0.5] * 32, fp8=True, stream=s),
-    "dsa_hot_plan": lambda m, s: m.dsa_hot_plan(gpu(NQ, K, dtype=I32), _batch(), _state(), 0, stream=s),
-    "dsa_hot_fetch": lambda m, s: m.dsa_hot_fetch(_state(), _batch(), [gpu(64, 576)], [gpu(8, 576)], stream=s),
-    "indexshare_group_forward": lambda m, s: m.indexshare_group_forward(_group(), _batch(), stream=s),
-    "indexshare_group_forward_hot": lambda m, s: m.indexshare_group_forward_hot(
-        _group(), _batch(), _hot(m), 0, stream=s),
+    "dsa_indexer_scores": lambda m, s, **k: m.dsa_indexer_scores(
+        gpu(NQ, 32, 128), gpu(NQ, 32, dtype=F32), gpu(64, 128), _batch(), stream=s, **k),
+    "dsa_topk": lambda m, s, **k: m.dsa_topk(gpu(NQ, 128, dtype=F32), _batch(), K, stream=s, **k),
+    "dsa_sparse_mla_attn": lambda m, s, **k: m.dsa_sparse_mla_attn(
+        gpu(NQ, H, 512), gpu(NQ, H, 64), gpu(64, 576), gpu(NQ, K, dtype=I32), _batch(), scale=1.0, stream=s, **k),
+    "dsa_sparse_mla_attn_rows": lambda m, s, **k: m.dsa_sparse_mla_attn_rows(
+        gpu(NQ, H, 512), gpu(NQ, H, 64), gpu(64, 576), gpu(NQ, K, dtype=I32), _batch(), scale=1.0, stream=s, **k),
+    "dsa_kv_fp8_quantize": lambda m, s, **k: m.dsa_kv_fp8_quantize(gpu(NQ, 576), stream=s, **k),
+    "dsa_kv_int4_quantize": lambda m, s, **k: m.dsa_kv_int4_quantize(gpu(NQ, 576), stream=s, **k),
+    "dsa_kv_append": lambda m, s, **k: m.dsa_kv_append(gpu(NQ, 576), *_entries(), _batch(), gpu(64, 576), stream=s, **k),
+    "dsa_kv_read": lambda m, s, **k: m.dsa_kv_read(gpu(64, 576), *_entries(), _batch(), stream=s, **k),
+    "dsa_fp8_quantize": lambda m, s, **k: m.dsa_fp8_quantize(gpu(NQ, 128), stream=s, **k),
+    "dsa_indexer_append_keys": lambda m, s, **k: m.dsa_indexer_append_keys(
+        gpu(NQ, 128), *_entries(), _batch(), gpu(64, 128), [0.5] * 32, stream=s, **k),
+    "dsa_indexer_prepare_queries": lambda m, s, **k: m.dsa_indexer_prepare_queries(
+        gpu(NQ, 32, 128), _batch(), [0.5] * 32, fp8=True, stream=s, **k),
+    "dsa_hot_plan": lambda m, s, **k: m.dsa_hot_plan(gpu(NQ, K, dtype=I32), _batch(), _state(), 0, stream=s, **k),
+    "dsa_hot_fetch": lambda m, s, **k: m.dsa_hot_fetch(_state(), _batch(), [gpu(64, 576)], [gpu(8, 576)], stream=s, **k),
+    "indexshare_group_forward": lambda m, s, **k: m.indexshare_group_forward(_group(), _batch(), stream=s, **k),
+    "indexshare_group_forward_hot": lambda m, s, **k: m.indexshare_group_forward_hot(
+        _group(), _batch(), _hot(m), 0, stream=s, **k),
 }
 
 
@@ -190,3 +193,80 @@ def test_append_without_a_workspace_reports_its_entries(dsa, monkeypatch, given,
     m.dsa_kv_append(gpu(NQ, 576), *_entries(), _batch(), gpu(64, 576), ws=ws, stream=STREAM)
     assert dsa.reached == ["dsa_kv_append"] and len(seen) == fetched
     assert all(s is STREAM for _, s in seen)
+
+
+# ---------------------------------------------------------------- what the other calls are given
+@pytest.mark.parametrize("bad", [lambda: torch.zeros(4096, dtype=U8), lambda: gpu(8192, dtype=U8)[::2]],
+                         ids=["on the host", "with gaps"])
+@pytest.mark.parametrize("name", sorted(set(CALLS) - {"dsa_kv_fp8_quantize", "dsa_kv_int4_quantize",
+                                                      "dsa_fp8_quantize"}))
+def test_workspaces_are_checked(dsa, monkeypatch, name, bad):
+    made = lambda stream, make, *a, **k: gpu(*a[0], dtype=k["dtype"])  # noqa: E731
+    monkeypatch.setattr(dsa.m, "_made", made)
+    CALLS[name](dsa.m, STREAM, ws=gpu(4096, dtype=U8))
+    reached = list(dsa.reached)
+    assert reached
+    with pytest.raises(ValueError):
+        CALLS[name](dsa.m, STREAM, ws=bad())
+    assert dsa.reached == reached
+
+
+def _raises(dsa, call):
+    with pytest.raises(ValueError):
+        call()
+    assert not dsa.reached
+
+
+def test_quantiser_outputs_are_checked(dsa):
+    x, codes, scale = gpu(NQ, 128), gpu(NQ, 128, dtype=U8), gpu(NQ, dtype=F32)
+    dsa.m.dsa_fp8_quantize(x, codes, scale, stream=STREAM)
+    dsa.m.dsa_fp8_quantize(x, codes.reshape(-1), scale, stream=STREAM)
+    dsa.reached.clear()
+    _raises(dsa, lambda: dsa.m.dsa_fp8_quantize(x, codes[1:], scale, stream=STREAM))
+    _raises(dsa, lambda: dsa.m.dsa_fp8_quantize(x, codes, scale[1:], stream=STREAM))
+
+
+def test_key_append_and_query_preparation_are_checked(dsa):
+    ws, f = gpu(4096, dtype=U8), [0.5] * 32
+    _raises(dsa, lambda: dsa.m.dsa_indexer_append_keys(gpu(NQ, 128), *_entries(), _batch(), gpu(64, 64), f, ws=ws,
+                                                       stream=STREAM))
+    q, out = gpu(NQ, 32, 128), gpu(NQ, 32, 128, dtype=U8)
+    for scale in (gpu(NQ - 1, 32, dtype=F32), gpu(NQ, 32), torch.zeros((NQ, 32))):
+        _raises(dsa, lambda: dsa.m.dsa_indexer_prepare_queries(q, _batch(), f, fp8=True, q_out=out, q_scale=scale,
+                                                               ws=ws, stream=STREAM))
+
+
+def test_hot_calls_are_checked(dsa):
+    m, ws, small = dsa.m, gpu(4096, dtype=U8), _state()
+    small.num_seqs = 0
+    rows = gpu(NQ, K, dtype=I32)
+    _raises(dsa, lambda: m.dsa_hot_plan(gpu(NQ - 1, K, dtype=I32), _batch(), _state(), 0, rows, ws=ws, stream=STREAM))
+    _raises(dsa, lambda: m.dsa_hot_plan(gpu(NQ, K, dtype=I32), _batch(), small, 0, rows, ws=ws, stream=STREAM))
+    _raises(dsa, lambda: m.dsa_hot_fetch(small, _batch(), [gpu(64, 576)], [gpu(0, 576)], ws=ws, stream=STREAM))
+    hot = _hot(m)
+    hot.spans = [small]
+    _raises(dsa, lambda: m.indexshare_group_forward_hot(_group(), _batch(), hot, 0, rows, ws=ws, stream=STREAM))
+    with pytest.raises(ValueError):
+        m.HotGroup([], [gpu(64, 576), gpu(63, 576)], num_q=NQ, k=K, device="cpu")
+
+
+def test_groups_are_checked(dsa):
+    m, ws, few = dsa.m, gpu(4096, dtype=U8), _group()
+    few.num_q = NQ - 1
+    idx = gpu(NQ, K, dtype=I32)
+    _raises(dsa, lambda: m.indexshare_group_forward(few, _batch(), idx, ws=ws, stream=STREAM))
+    _raises(dsa, lambda: m.indexshare_group_forward_hot(few, _batch(), _hot(m), 0, idx, ws=ws, stream=STREAM))
+    layer = dict(q_lat=gpu(NQ, H, 512), q_rope=gpu(NQ, H, 64), kv=gpu(64, 576), q_idx=gpu(NQ, 32, 128, dtype=U8),
+                 w=gpu(NQ, 32, dtype=F32), k_idx=gpu(64, 128, dtype=U8), q_scale=gpu(NQ, 32, dtype=F32),
+                 k_scale=gpu(64, dtype=F32))
+    make = lambda out, **k: m.Group("F", [dict(layer, **k)], k=K, scale=1.0, outs=out)  # noqa: E731
+    make([gpu(NQ, H, 512)])
+    for out in ([gpu(NQ - 1, H, 512)], [gpu(NQ, H, 512, dtype=F32)], [torch.zeros((NQ, H, 512), dtype=torch.bfloat16)], []):
+        with pytest.raises(ValueError):
+            make(out)
+    with pytest.raises(ValueError):
+        make([gpu(NQ, H, 512)], k_scale=gpu(63, dtype=F32))
+
+
+def test_a_batch_on_the_host_has_no_device_number(dsa):
+    assert dsa.m.Batch([0, 1], [0], [0], 128, device=torch.device("cpu", 0)).device.index is None
