@@ -286,6 +286,10 @@ __global__ void __launch_bounds__(MlaCfg<H>::NT, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------ softmax: key = TMEM lane, HW heads
+    // After a wait that ran out these warps go on all the same, without the copies that
+    // it was for: each comes to every barrier that they share, while one that left its
+    // loop could leave the others at a barrier for good.  (2560 queries of 16 heads 617 ->
+    // 621 us; leaving together by votes and flags cost the 8K prefill 1.6 to 2.2%.)
     const int quarter = warp & 3;              // TMEM lane quarter this warp may access
     const int h0 = (warp >> 2) * HW;           // first head of this warp
     const int key = quarter * 32 + lane;       // key of the block (= TMEM lane)
@@ -502,7 +506,7 @@ __global__ void __launch_bounds__(MlaCfg<H>::NT, 1)
         const int64_t rr = row_of(e);
         valid = rr >= 0 && rr < p.kv_rows;
       }
-      if (!mbar_wait(bar(B_S), u & 1, abort_flag, p.status, to)) break;
+      mbar_wait(bar(B_S), u & 1, abort_flag, p.status, to);
       tc_fence_after();
       // d = scale*log2(e)*s - m: the exponent of P and the rescale test in one FFMA
       float d[HW];
@@ -603,12 +607,12 @@ __global__ void __launch_bounds__(MlaCfg<H>::NT, 1)
         // refill for block j+1: chunk c of P.V frees sub-tiles 2c, 2c+1 (the
         // last one also the RoPE sub-tile holding P)
         resolve_rows();
-        bool alive = true;
+        bool freed = true;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-          const bool freed = mbar_wait(bar(B_CFREE + c), u & 1, abort_flag, p.status, to);
+          freed = mbar_wait(bar(B_CFREE + c), u & 1, abort_flag, p.status, to);
           if (!(KV8 ? __all_sync(0xffffffffu, freed) : freed)) {
-            alive = false;
+            freed = false;
             break;
           }
           if constexpr (KV8) {
@@ -621,8 +625,7 @@ __global__ void __launch_bounds__(MlaCfg<H>::NT, 1)
             signal(c);
           }
         }
-        if (!alive) break;
-        if constexpr (KV8) convert8(3, 0);
+        if (KV8 && freed) convert8(3, 0);
         if (j + 2 < j1) prefetch_rows();
       }
     }
@@ -636,7 +639,7 @@ __global__ void __launch_bounds__(MlaCfg<H>::NT, 1)
     // or for a token split over 4 to 16 CTAs written with the running maxima
     // and the row sums to the token's partial results in global memory
     // (zeros for a CTA without blocks), which the cluster combines through L2
-    const bool have = j1 > j0 && mbar_wait(bar(B_O), 0, abort_flag, p.status, to);
+    const bool have = j1 > j0 && __all_sync(0xffffffffu, mbar_wait(bar(B_O), 0, abort_flag, p.status, to));
     tc_fence_after();
     float* Od = kMergeL2 ? p.part + (static_cast<int64_t>(t) * NSPLIT + rank) * (H * 512 + 2 * H)
                          : reinterpret_cast<float*>(sm + C::OFF_C);
@@ -1069,9 +1072,10 @@ __global__ void __launch_bounds__(MlaCfg<H>::NT + 64, 1)
       }
       e_next = key < nv ? ld_stream_i32(irow + key) : -1;
     }
-    bool alive = true;
+    // (after a wait that ran out: as in the kernel above, and without waiting in the many
+    // blocks that may be left; 8192 queries 2527 -> 2534 us)
 #pragma unroll 1
-    for (int i = 0; alive && i < ntok; ++i) {
+    for (int i = 0; i < ntok; ++i) {
       const int4 tk = toks[i];  // (its token index is read again where it is used)
       const int pos = tk.y;
       const int nvalid = min(p.K, pos + 1), nb = (nvalid + 127) / 128;
@@ -1109,10 +1113,8 @@ __global__ void __launch_bounds__(MlaCfg<H>::NT + 64, 1)
           else if (has_next)
             resolve_rows(toks[i + 1]);
         }
-        if (!mbar_wait(bar(B_S), gu & 1, abort_flag, p.status, to)) {
-          alive = false;
-          break;
-        }
+        const bool dead = *abort_flag;
+        if (!dead) mbar_wait(bar(B_S), gu & 1, abort_flag, p.status, to);
         tc_fence_after();
         float d[HW];
         tmem_cols_load<HW>(lane_base + C::TM_S + h0, d);
@@ -1201,19 +1203,14 @@ __global__ void __launch_bounds__(MlaCfg<H>::NT + 64, 1)
           }
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            if (!mbar_wait(bar(B_CFREE + c), gu & 1, abort_flag, p.status, to)) {
-              alive = false;
-              break;
-            }
+            if (dead || !mbar_wait(bar(B_CFREE + c), gu & 1, abort_flag, p.status, to)) break;
             issue(2 * c);
             issue(2 * c + 1);
             if (c == 3) issue(8);
             signal(c);
           }
-          if (!alive) break;
         }
       }
-      if (!alive) break;
       // ---- the token's output: row sums, then O^T / L from TMEM to global memory
       head_reduce<HW, 16, false>(lpart, lane);
       red[quarter * H + h0 + lane] = lpart[0];
@@ -1226,10 +1223,7 @@ __global__ void __launch_bounds__(MlaCfg<H>::NT + 64, 1)
         m_used[tid] = -INFINITY;  // the next token's running maximum
       }
       named_bar_sync(1, NST);
-      if (!mbar_wait(bar(B_O), i & 1, abort_flag, p.status, to)) {
-        alive = false;
-        break;
-      }
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(B_O), i & 1, abort_flag, p.status, to))) continue;
       tc_fence_after();
       // dims 128c + key of this thread's 32 heads: lanes 2m and 2m+1 swap one
       // value of each head pair, so that each writes one head's two dims
