@@ -386,7 +386,12 @@ void dsa_launch_counts_reset(void) {
   for (auto& c : g_launches) c.store(0);
 }
 
-void dsa_set_wait_timeout_ns(uint64_t ns) { g_timeout_ns.store(ns); }
+void dsa_set_wait_timeout_ns(uint64_t ns) {
+  // A CTA that gives up waits with the same limit for its own copies and products before
+  // it exits: a few microseconds, which a shorter limit would cut off.
+  constexpr uint64_t kLeast = 1000000;
+  g_timeout_ns.store(ns < kLeast ? kLeast : ns);
+}
 
 void dsa_set_mla_persistent(int on) { set_mla_persistent(on != 0); }
 

@@ -164,7 +164,9 @@ DSA_API void dsa_profile_enable(int on);
 DSA_API int dsa_profile_collect(double* ms, uint64_t* launches, int n);
 
 /* Upper bound in nanoseconds on every spin-wait inside the kernels launched
- * after this call (default 2e9).  Exposed so that tests can shorten it. */
+ * after this call (default 2e9; less than 1e6 is taken as 1e6, as a CTA that gives up
+ * waits with this limit for its own copies in flight).  Exposed so that tests can
+ * shorten it. */
 DSA_API void dsa_set_wait_timeout_ns(uint64_t ns);
 
 /* Kernel choice for sparse attention over many tokens (at least twice as many

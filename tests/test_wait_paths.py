@@ -58,3 +58,27 @@ def test_softmax_warps_come_to_every_barrier_together(name, kernels):
         # nor is a loop's count a matter of a wait
         for m in re.finditer(r"\bfor \(([^;]*);([^;]*);", role):
             assert not re.search(r"\b(alive|dead|ok)\b|wait", m.group(2)), m.group(0)
+
+
+@pytest.mark.gpu
+def test_the_wait_limit_leaves_time_for_what_is_in_flight():
+    """A CTA that gives up waits for its own copies and products with the same limit, so a
+    limit below a millisecond is taken as one: a wait for nothing takes that long."""
+    torch = pytest.importorskip("torch")
+    dsa = pytest.importorskip("dsa_indexer_indexshare_gb300")
+    ws = dsa.workspace(256, torch.device("cuda:0"))
+    try:
+        for ns in (0, 1, 1000):
+            dsa.set_wait_timeout_ns(ns)
+            a, b = torch.cuda.Event(True), torch.cuda.Event(True)
+            torch.cuda.synchronize()
+            a.record()
+            dsa.dsa_selftest_wait_timeout(ws)
+            b.record()
+            with pytest.raises(dsa.DsaError) as e:
+                dsa.status_fetch(ws)
+            assert e.value.status == dsa.DSA_ERR_TIMEOUT
+            torch.cuda.synchronize()
+            assert a.elapsed_time(b) >= 0.99
+    finally:
+        dsa.set_wait_timeout_ns(2_000_000_000)
