@@ -19,8 +19,8 @@
 // power 0.0094 against 0.0102 in groups of 32 normal values, both with bf16
 // scales) and widen in fewer operations.
 //
-// All kernels give one warp to a row; lane l holds dims 8l .. 8l+7 and
-// 256+8l .. 256+8l+7, so that every access of a warp is one contiguous run.
+// The append and the quantiser give a warp one row, the read-back two; lane l holds dims
+// 8l .. 8l+7 and 256+8l .. 256+8l+7, so that every access of a warp is one contiguous run.
 // Bound by HBM: the append reads 1152 bytes a row and writes 416 / 656 / 1152,
 // the read-back the other way round.  Measured (times in a graph): the read-back of
 // 131,072 INT4 rows in 32.4 us, 6.36 TB/s or 0.95 of the copy rate; of 16,301 INT4
@@ -107,13 +107,13 @@ __device__ __forceinline__ uint32_t int4_word(const uint4& w, uint16_t& scale_bi
 // Eight E4M3 codes and their group's scale; the group is 16 lanes.  The scale is
 // the fp32 nearest to amax / 448, as in every FP8 row (kv_fp8_quant_kernel): a
 // cache may hold rows of both calls.  (The product amax * fp32(1/448) would be an ulp off
-// in six groups of ten; 4503 rows take 5.59 us with it and 5.71 with the division.)  A code is the E4M3 value nearest to
-// the exact x / sc (one element in 200 of a random group is an exact midpoint, so
-// it is decided for all): q = |x| * (1/sc) gives the interval between two codes,
-// m is its midpoint, the sign of the fma |x| - m sc is that of |x| / sc - m
-// exactly, and m or its neighbour on that side is what the conversion rounds.
-// (Where q is off by so little that it lies in the next interval, |x| / sc is that
-// close to their common code, which either gives.)  Extreme scales go out of line.
+// in six groups of ten; 4503 rows take 5.59 us with it and 5.71 with the division.)
+// A code is the E4M3 value nearest to the exact x / sc (one element in 200 of a random
+// group is an exact midpoint, so it is decided for all): q = |x| * (1/sc) gives the
+// interval between two codes, m is its midpoint, the sign of the fma |x| - m sc is that
+// of |x| / sc - m exactly, and m or its neighbour on that side is what the conversion
+// rounds.  (Where q is off by so little that it lies in the next interval, |x| / sc is
+// that close to their common code, which either gives.)  Extreme scales go out of line.
 static __device__ __noinline__ uint32_t e4m3_exact(float x, float sc) { return e4m3_of_quotient(x, sc); }
 
 __device__ __forceinline__ uint2 fp8_codes8(const uint4& w, float& sc) {

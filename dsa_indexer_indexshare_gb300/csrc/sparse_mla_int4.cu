@@ -37,15 +37,16 @@
 // One CTA per SM walks a list of tokens (many tokens), or a cluster of NSPLIT
 // CTAs shares the blocks of one token (decode).
 //
-// Measured (64 heads, K = 2048): 8192 queries of one sequence in 2.51 ms (the bf16
-// kernel 2.52 ms; 2.04e12 operations, 43% of the cuBLAS rate), a decode step of 64
-// tokens in 37 us (bf16 rows 52 us).  A block of 128 keys takes about 6900 cycles of
-// an SM, three times its 68 MMAs.  The widening bounds it: 68 slot fills of a warp,
-// 105 instructions each (four warps of a scheduler fill a slot in 550 cycles
+// Measured (64 heads, K = 2048; in a replayed graph): 8192 queries of one sequence in
+// 2.51 ms (the bf16 kernel 2.54 ms; 2.04e12 operations, 43% of the cuBLAS rate), a decode
+// step of 64 tokens in 37.5 us (bf16 rows 43.3 us; 45 and 53 us after a flush of L2), of 8
+// tokens in 19.0 us (16.1 us).  A block of 128 keys takes about 6900 cycles of
+// an SM, three times its 68 MMAs.  The widening bounds it: 68 slot fills of a warp
+// (four warps of a scheduler fill a slot in 550 cycles
 // side by side, one alone in 300), and about 190 cycles around each fill to find
-// the slot free and to announce it.  2560 queries take 590 us: 13% less without the
-// arithmetic of the widening, 27% less without its stores, 9% without the MMAs, 1%
-// without the exponentials; slots of half the size cost 25%, and neither an earlier
+// the slot free and to announce it.  Of the 600 us that 2560 queries took when parts were
+// left out, the arithmetic of the widening was 13%, its stores 27%, the MMAs 9%, the
+// exponentials 1% (590 us now); slots of half the size cost 25%, and neither an earlier
 // release of S^T, nor P in two halves, nor fewer looks at the barriers gain any.
 #include <cuda_bf16.h>
 
