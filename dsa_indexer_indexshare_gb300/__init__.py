@@ -9,6 +9,7 @@ been built, and a call fails if its kernel cannot run.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import struct
 from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_int64, c_size_t, c_uint64, c_void_p
@@ -184,6 +185,17 @@ def _addr(t, name, dtype, device, shape):
     if not (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == device.index
             and t.shape == shape and t.is_contiguous()):
         _need(t, name, dtype, device, shape)
+    return t.data_ptr()
+
+
+def _room(t, name, dtype, device, shape):
+    """Address of an output that may be larger than the call fills (a buffer for the
+    largest batch), in any shape."""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == device.index
+            and t.shape == shape and t.is_contiguous()):
+        _need(t, name, dtype, device)
+        if t.numel() < math.prod(shape):
+            raise ValueError(f"{name} has {t.numel()} entries, want at least {tuple(shape)}")
     return t.data_ptr()
 
 
@@ -395,7 +407,7 @@ def dsa_sparse_mla_attn(q_lat, q_rope, kv, idx, batch: Batch, *, scale: float, o
     po = _addr(out, "out", torch.bfloat16, dev, (nq, H, LATENT))
     if lse is None and with_lse:
         lse = _made(stream, torch.empty, (nq, H), dtype=torch.float32, device=dev)
-    pl = None if lse is None else _addr(lse, "lse", torch.float32, dev, (nq, H))
+    pl = None if lse is None else _room(lse, "lse", torch.float32, dev, (nq, H))
     if ws is None:
         ws = _made(stream, workspace, lib.dsa_sparse_mla_workspace_size(batch.c, H, k), dev)
     _check(_ATTN[dt](pq, pr, pkv, kv.shape[0], pi, k, H, float(scale), batch._ref, po, pl, *_ws(ws, dev),
@@ -448,7 +460,7 @@ def dsa_kv_append(kv_new, kv_seq, kv_pos, batch: Batch, kv, inv_freq=None, *, ws
     dev = batch.device
     if not isinstance(kv_new, torch.Tensor):
         raise TypeError("kv_new must be a tensor")
-    if kv_new.device != dev or kv_new.dtype is not torch.bfloat16:
+    if kv_new.get_device() != dev.index or kv_new.dtype is not torch.bfloat16:
         raise ValueError(f"kv_new must be a bfloat16 tensor on {dev}")
     if kv_new.dim() != 2:
         raise ValueError("kv_new must be [n, >= 576] with contiguous rows")
@@ -530,7 +542,7 @@ class Group:
         if len(self.outs) != nl:
             raise ValueError("one output per layer")
         for l, o in enumerate(self.outs):
-            _need(o, f"outs[{l}]", torch.bfloat16, dev, (num_q, H, LATENT))
+            _room(o, f"outs[{l}]", torch.bfloat16, dev, (num_q, H, LATENT))
         self.lses = [torch.empty((num_q, H), dtype=torch.float32, device=dev)
                      for _ in range(nl)] if with_lse else None
 
@@ -597,10 +609,8 @@ def dsa_fp8_quantize(x, codes=None, scale=None, *, stream=None):
         codes = _made(stream, torch.empty, x.shape, dtype=torch.uint8, device=x.device)
     if scale is None:
         scale = _made(stream, torch.empty, x.shape[:-1], dtype=torch.float32, device=x.device)
-    _need(codes, "codes", torch.uint8, x.device)
-    _need(scale, "scale", torch.float32, x.device)
-    if codes.numel() < x.numel() or scale.numel() < rows:
-        raise ValueError(f"codes and scale must hold {x.numel()} and {rows} entries")
+    _room(codes, "codes", torch.uint8, x.device, x.shape)
+    _room(scale, "scale", torch.float32, x.device, x.shape[:-1])
     _check(lib.dsa_fp8_quantize(_ptr(x), rows, _ptr(codes), _ptr(scale), _stream(stream, x.device)),
            "dsa_fp8_quantize")
     return codes, scale
@@ -659,7 +669,7 @@ def dsa_indexer_prepare_queries(q_new, batch: Batch, inv_freq, *, fp8=False, q_o
         q_scale = _made(stream, torch.empty, (batch.num_q, INDEX_HEADS), dtype=torch.float32, device=dev)
     _need(q_out, "q_out", torch.uint8 if fp8 else torch.bfloat16, dev, tuple(q_new.shape))
     if fp8:
-        _need(q_scale, "q_scale", torch.float32, dev, (batch.num_q, INDEX_HEADS))
+        _room(q_scale, "q_scale", torch.float32, dev, (batch.num_q, INDEX_HEADS))
     if ws is None:
         ws = _made(stream, workspace, STATUS_BYTES, dev)
     _check(lib.dsa_indexer_prepare_queries(_ptr(q_new), batch.c, DSA_FP8_E4M3 if fp8 else DSA_BF16,
@@ -788,11 +798,11 @@ def dsa_sparse_mla_attn_rows(q_lat, q_rope, kv, rows, batch: Batch, *, scale: fl
     pi, k = _index_list(rows, "rows", batch.num_q, dev)
     if out is None:
         out = _made(stream, torch.empty, (batch.num_q, H, LATENT), dtype=torch.bfloat16, device=dev)
-    _need(out, "out", torch.bfloat16, dev, (batch.num_q, H, LATENT))
+    _room(out, "out", torch.bfloat16, dev, (batch.num_q, H, LATENT))
     if lse is None and with_lse:
         lse = _made(stream, torch.empty, (batch.num_q, H), dtype=torch.float32, device=dev)
     if lse is not None:
-        _need(lse, "lse", torch.float32, dev, (batch.num_q, H))
+        _room(lse, "lse", torch.float32, dev, (batch.num_q, H))
     if ws is None:
         ws = _made(stream, workspace, lib.dsa_sparse_mla_workspace_size(batch.c, H, k), dev)
     _check(lib.dsa_sparse_mla_attn_rows(_ptr(q_lat), _ptr(q_rope), _ptr(kv), kv.shape[0],
@@ -811,8 +821,9 @@ class HotGroup:
         self.cold_kv = list(cold_kv)
         for l, t in enumerate(self.cold_kv):
             _cold(t, f"cold_kv[{l}]")
-            if t.dtype != self.cold_kv[0].dtype or t.shape != self.cold_kv[0].shape:
-                raise ValueError("cold caches must share dtype and shape")
+            first = self.cold_kv[0]
+            if t.dtype != first.dtype or t.shape[1:] != first.shape[1:] or t.shape[0] < first.shape[0]:
+                raise ValueError("cold caches must share dtype and width, and hold the rows of the first")
         self.rows = torch.empty((num_q, k), dtype=torch.int32, device=device)
         self._spans = (_Hot * len(self.spans))(*[s._c for s in self.spans])
         self._cold = (c_void_p * len(self.cold_kv))(*[t.data_ptr() for t in self.cold_kv])

@@ -69,12 +69,14 @@ def test_attention_takes_what_it_needs(dsa, name, kind):
     out, lse = _attention(name, dsa, kind)
     assert out.shape == (NQ, H, 512) and lse.shape == (NQ, H) and len(dsa.reached) == 1
     _attention(name, dsa, kind, idx=gpu(NQ + 3, K, dtype=torch.int32))  # rows behind the batch's are not read
+    _attention(name, dsa, kind, lse=gpu(NQ + 3, H, dtype=torch.float32))  # and of a larger buffer not written
+    _attention(name, dsa, kind, lse=gpu(NQ * H, dtype=torch.float32))
+    assert len(dsa.reached) == 4
 
 
 @pytest.mark.parametrize("bad", [
     dict(lse=gpu(NQ, H)),                                          # 2 bytes a value
     dict(lse=gpu(NQ - 1, H, dtype=torch.float32)),                 # too short
-    dict(lse=gpu(NQ * H, dtype=torch.float32)),
     dict(lse=gpu(NQ, 2 * H, dtype=torch.float32)[:, ::2]),         # not contiguous
     dict(lse=torch.zeros((NQ, H))),                                # on the host
     dict(ws=torch.zeros(4096, dtype=torch.uint8)),
@@ -261,6 +263,7 @@ def test_groups_are_checked(dsa):
                  k_scale=gpu(64, dtype=F32))
     make = lambda out, **k: m.Group("F", [dict(layer, **k)], k=K, scale=1.0, outs=out)  # noqa: E731
     make([gpu(NQ, H, 512)])
+    make([gpu(NQ + 2, H, 512)])
     for out in ([gpu(NQ - 1, H, 512)], [gpu(NQ, H, 512, dtype=F32)], [torch.zeros((NQ, H, 512), dtype=torch.bfloat16)], []):
         with pytest.raises(ValueError):
             make(out)
